@@ -217,6 +217,7 @@ struct Row {
   float top;        // largest logit
   float none;       // a value whose weight rounds to zero, kLowest if there is none
   float light_c, light_rest;  // see light
+  float heavy;      // tokens below weigh light (kLowest: none does)
   float ch, cl;     // log2(e) / temperature as a pair
   // what is left: at least thr, and past the cut: key above it, or equal with an index up to cut_idx
   float thr, below;  // below: upper end (not included) while a bracket is open
@@ -400,6 +401,10 @@ struct Row {
     *rest = static_cast<uint32_t>(r64 >> 32);
     return static_cast<uint64_t>(static_cast<uint32_t>(w)) * hi + sum;
   }
+  // The weight of a token that can be drawn: one form, by its logit alone, for every sum and every
+  // cut.  All sums are then sums of the same integers, and where a cut falls does not depend on
+  // which of the passes below found it.
+  __device__ __forceinline__ uint64_t mass(float v) const { return v < heavy ? light(fmaxf(v, none)) : weight(v); }
   // sum and four of them, two at a time in the float operations (the rests: below 2^30 each)
   __device__ __forceinline__ uint64_t light4(const float* v, uint64_t sum) const {
     const uint64_t c = pair(light_c, light_c), h = pair(ch, ch), l = pair(cl, cl), off = pair(-light_rest, -light_rest);
@@ -423,7 +428,7 @@ struct Row {
   // missing.  Of values equal to low those past index `upto` do not count.  `seen(values, first
   // index)` gets every vector.
   template <typename F, typename O>
-  __device__ __forceinline__ void masses(float low, int upto, float heavy, float pick, uint64_t& sum, F&& dense, O&& seen) {
+  __device__ __forceinline__ void masses(float low, int upto, float pick, uint64_t& sum, F&& dense, O&& seen) {
     constexpr int S = 8 / N;  // vectors of a lane in a step
     const int its = steps_of_run(), end = inner();
     const float above = from_key(key_of(low) + 1u);
@@ -623,7 +628,7 @@ struct Row {
       const bool mine = tid < n_all && alive(s.fv[min(tid, kCap - 1)], s.fi[min(tid, kCap - 1)]);
       if (tid < n_all) {
         s.few_key[tid] = mine ? key_of(s.fv[tid]) : 0;
-        if (MASS) s.few_w[tid] = mine ? weight(s.fv[tid]) : 0;
+        if (MASS) s.few_w[tid] = mine ? mass(s.fv[tid]) : 0;
       }
       __syncthreads();
       if (mine) {
@@ -658,7 +663,7 @@ struct Row {
         if ((k & mask) != prefix) return;
         const int b = (k >> shift) & 255;
         atomicAdd(&s.cnt[slot_of(b)], 1u);
-        if (MASS) add_mass(b, weight(v));
+        if (MASS) add_mass(b, mass(v));
       });
       find<MASS>(true, want);
       if (s.f_bin < 0) return;  // all of them together stay below `want`: no cut
@@ -669,7 +674,7 @@ struct Row {
     const int ties = s.f_cnt;
     uint64_t quota = want;
     if (MASS) {
-      const uint64_t w = weight(from_key(prefix));
+      const uint64_t w = mass(from_key(prefix));
       quota = (want + w - 1) / w;
     }
     const int idx = quota >= static_cast<uint64_t>(ties) ? kNone : nth_tie(prefix, static_cast<int>(quota));
@@ -830,7 +835,7 @@ struct Row {
   // are said to be few, lists them: where they fit and the cut is one of them, `listed` is set and
   // `want` counts from the top.
   template <bool MASS>
-  __device__ __forceinline__ void narrow(uint64_t* want, float keep, float heavy, float pick, bool few) {
+  __device__ __forceinline__ void narrow(uint64_t* want, float keep, float pick, bool few) {
     float lo = MASS ? fmaxf(pick, level(46.5f)) : fmaxf(top - 32.f, kLowest), hi = top;
     const float least = MASS ? level(46.5f) : kLowest;  // no weight below
     uint64_t sum = 0;
@@ -861,7 +866,7 @@ struct Row {
       if (whole && heavy > kLowest) {
         // the picked ones in a list too: mostly the cut is among them
         thr = pick;
-        masses(none, kNone, heavy, pick, sum, dense, [&](const float* v, int i) { note(v, i, n); });
+        masses(none, kNone, pick, sum, dense, [&](const float* v, int i) { note(v, i, n); });
       } else if (uncounted) {
         // All light tokens, too many for a queue to gain anything.  Sums in 16 copies, a lane's by its
         // number (two lanes meet at most), in two words that need no carry: weights below 2^34 in
@@ -1007,7 +1012,7 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
   const int part = rank * kWarps + warp, parts = ranks * kWarps;
   R r{s, x0 - mis, p.V, mis, rank, ranks,
       static_cast<int>(static_cast<int64_t>(nvec) * part / parts), static_cast<int>(static_cast<int64_t>(nvec) * (part + 1) / parts),
-      tid, warp, lane, false, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, kLowest, INFINITY, 0u, kNone, false, 0, 0, 0};
+      tid, warp, lane, false, 0.f, 0.f, 0.f, 0.f, kLowest, 0.f, 0.f, kLowest, INFINITY, 0u, kNone, false, 0, 0, 0};
   for (int e = tid; e < 64 * 32; e += kThreads) {
     const uint64_t t = table.t[e >> 5];
     const uint32_t hi = static_cast<uint32_t>((t + 0x2000u) >> 14);
@@ -1096,7 +1101,7 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
   r.none = r.level(45.9f);
   const float top2 = r.top * r.ch, reach = fmaxf(fabsf(r.top), fabsf(r.none)) * r.ch;
   const bool lights = r.none > kLowest && reach < 16384.f;
-  const float heavy = lights ? r.level(p.min_p && min_p > 0.f ? kLightOctavesMinP : kLightOctaves) : kLowest;
+  const float heavy = r.heavy = lights ? r.level(p.min_p && min_p > 0.f ? kLightOctavesMinP : kLightOctaves) : kLowest;
   const float pick = lights ? fminf(heavy, r.level(kPickOctaves)) : kLowest;
   {
     const float grid = rintf(top2 * 64.f) * 0.015625f;
@@ -1116,7 +1121,7 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
       // all tokens from `below` up are kept: their sum in the same pass
       int n = 0;
       const uint64_t counted = r.light(heavy);
-      r.masses(r.below, kNone, heavy, heavy, kept_sum, [&](float v, bool valid) {
+      r.masses(r.below, kNone, heavy, kept_sum, [&](float v, bool valid) {
         if (valid) kept_sum += r.weight(v) - counted;
       }, [&](const float* v, int i) { r.note(v, i, n); });
       r.gather(n);
@@ -1166,13 +1171,13 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
       const float d = (s.f_bin + 1) * 0.125f;
       r.thr = fmaxf(r.top - d - (fabsf(r.top) + d) * 1e-6f, kLowest);
     } else {
-      r.template narrow<false>(&want, 0.f, kLowest, kLowest, false);
+      r.template narrow<false>(&want, 0.f, kLowest, false);
     }
     // (without effect when fewer than k tokens are above minus infinity)
     if (!cut_of(false, want)) return;
     if (use_p) {
       uint64_t sum = 0, total;
-      r.each([&](float v, int) { sum += r.weight(v); });
+      r.each([&](float v, int) { sum += r.mass(v); });
       for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
       __syncthreads();
       if (lane == 0) s.warp_sum[warp] = sum;
@@ -1190,7 +1195,7 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
 #pragma unroll
     for (int j = 0; j < kUnroll; ++j) met = met || best[j] >= pick;
     const bool few = __syncthreads_count(met) <= kThreads / 3;
-    r.template narrow<true>(&want, keep, heavy, pick, few);
+    r.template narrow<true>(&want, keep, pick, few);
     if (!cut_of(true, want)) return;
   } else if (min_p > 0.f) {
     r.thr = r.level(0.01f - log2f(min_p));
@@ -1205,9 +1210,8 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
   const uint64_t floor_w = min_p > 0.f ? part_of(1ull << kFrac, min_p, true) : 0;
   const bool all = !use_k && !use_p && min_p == 0.f;  // every token can be drawn
   auto kept = [&](float v, int i) { return all ? v > -INFINITY : r.alive(v, i); };
-  // (a token's weight is the same number in the sums and in the walk to it)
   auto weigh = [&](float v) -> uint64_t {
-    const uint64_t w = v < heavy ? r.light(fmaxf(v, r.none)) : r.weight(v);
+    const uint64_t w = r.mass(v);
     return w >= floor_w ? w : 0;
   };
   uint64_t before = 0, left = 0, total = 0;
@@ -1230,7 +1234,7 @@ __global__ void __launch_bounds__(warps_of(CL) * 32, 1)
         if (kept(s.lv[warp][e], s.li[warp][e])) sum += weigh(s.lv[warp][e]);
     } else if (min_p == 0.f && least < heavy) {
       const uint64_t counted = r.light(heavy);
-      r.masses(fmaxf(least, r.none), r.cut && least == from_key(r.cut) ? r.cut_idx : kNone, heavy, heavy, sum, [&](float v, bool valid) {
+      r.masses(fmaxf(least, r.none), r.cut && least == from_key(r.cut) ? r.cut_idx : kNone, heavy, sum, [&](float v, bool valid) {
         if (valid) sum += r.weight(v) - counted;
       }, [](const float*, int) {});
     } else {
