@@ -558,6 +558,9 @@ int fork_cache_append(const fork_cache* c, const fork_rope* rope, const uint16_t
  *   q, o [T_cap, Hq, d] bf16, contiguous (o may be q); kc, vc the layer's
  *   arrays; scale > 0.  Rows past the step's are left as they were.  A NaN or
  *   infinity in a key or value reaches the rows that see it and no others.
+ *   Scores, exponentials and sums are float32.  With max_new * Hq / Hkv of 16 at
+ *   most (32 for d = 64) a weight is multiplied to 2^-15 of itself, with more it is
+ *   rounded to bf16 (2^-8) first; the result is rounded to bf16 once.
  *   workspace: fork_cache_attn_workspace_bytes(c) bytes, 16-byte aligned, used
  *   by one call at a time; nothing in it has to be set, nothing is kept.
  * The keys are read in tiles of 128, split over the GPU's SMs in equal shares;

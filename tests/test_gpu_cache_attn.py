@@ -338,3 +338,37 @@ def test_a_wait_that_runs_out_is_reported_and_leaves_the_context_usable(F, torch
     F.fork_cache_attn(c, q, kc, vc, o)
     assert F.fork_cache_status(c) == 0
     assert torch.equal(o, clean)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,page,length,n_new,tree", [
+    (4, 1, 128, 16, [127, 128, 1, 383], [1, 1, 1, 1], False), (12, 4, 64, 64, [700, 5, 64], [3, 1, 5], True),
+    (8, 8, 128, 32, [9000, 40], [1, 1], False), (32, 1, 64, 16, [2000, 31, 0], [1, 1, 1], False),
+    (16, 2, 64, 32, [4001, 300], [4, 3], True), (7, 1, 128, 128, [600, 3], [2, 1], True)])
+def test_few_rows_carry_their_weights_in_more_than_bf16(F, torch, Hq, Hkv, d, page, length, n_new, tree):
+    """The kernel for few rows: a weight is the largest bf16 number below it and the bf16 of the rest, which is off by 2^-8
+    of at most 2^-7 of it; sums, scores and exponential within 2^-12 as in `check`; one rounding of the result."""
+    st = make_step(31, length, n_new, page, tree)
+    for sharp in (1.0, 3.0):
+        q, kc, vc = inputs(torch, st, Hq, Hkv, d, 5, sharp)
+        for window in (0, 100):
+            got, _ = run(F, torch, st, q, kc, vc, Hq, Hkv, d, window)
+            want, mag = reference(torch, st, q, kc, vc, window, d ** -0.5)
+            tol = want.abs() * 2.0 ** -8 + mag * (2.0 ** -15 + 2.0 ** -12) + 1e-30
+            err = (got.double() - want).abs()
+            assert bool((err <= tol).all()), float((err / tol).max())
+
+
+@pytest.mark.parametrize("max_new", [1, 8, 64])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("what", [float("inf"), float("-inf")])
+def test_an_infinity_that_every_row_sees(F, torch, max_new, d, what):
+    """In a tile without masked keys: the sum is that infinity, whatever the weight (1 where the queries are zero)."""
+    st = make_step(4, [1000, 300], [1, 1], 16, False, T_cap=64)
+    q, kc, vc = inputs(torch, st, 8, 2, d, 3)
+    for b, y in ((0, 5), (0, 700), (1, 130)):
+        vc[int(st["table"][b, y // 16]), :, y % 16, 3 + b] = what
+    for qq in (q, torch.zeros_like(q)):
+        got, _ = run(F, torch, st, qq, kc, vc, 8, 2, d, 0, None, max_new)
+        for b in range(2):
+            assert bool((got[b, :, 3 + b] == what).all())
+            assert bool(torch.isfinite(got[b, :, :3 + b]).all()) and bool(torch.isfinite(got[b, :, 4 + b:]).all())

@@ -406,9 +406,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float m_new = resc ? mt : m_used;
         const float at = m_new == -INFINITY ? 0.f : m_new;
         const float factor = resc ? ex2(m_used - at) : 1.f;
-        // rounded to bf16 for the product; the sum takes the rounded values, so that the rounding
+        // Rounded to bf16 for the product; the sum takes the rounded values, so that the rounding
         // cancels where one key carries the row (unrounded: 131 us for 135 us, and up to 1.4 times
-        // the error of the output's own rounding)
+        // the error of the output's own rounding).  The products bound this kernel: with a second one
+        // for what the rounding leaves, as the kernel for few rows has it, 131,000 keys x 256 rows
+        // take 184 us for 132, 16 requests x 64 nodes 137 for 99, prompt chunks 196 for 138; the
+        // relative error against 64 bits would fall from 0.0021 to 0.0017 (the result's rounding)
         const uint64_t sl2x2 = pair(sl2, sl2), atx2 = pair(-at, -at);
         float fs[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -420,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float lo, hi;
             unpair(fma2(pair(sv[i], sv[i + 1]), sl2x2, atx2), &lo, &hi);
             pk[e] = pack_bf16(ex2(lo), ex2(hi));
-add_halves(pk[e], &fs[e & 3], &fs[4 + (e & 3)]);
+            add_halves(pk[e], &fs[e & 3], &fs[4 + (e & 3)]);
           }
           tc::tmem_st16(ts + h * 16, pk);
         }
