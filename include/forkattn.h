@@ -498,7 +498,8 @@ int fork_cache_layout(const fork_cache* c, fork_cache_offsets* out);
  *     a ring state out of range or without room for the pages returned;
  *   FORK_STATUS_CAPACITY: more rows than T_cap, or too few free pages.
  * A parent outside [-1, i - 1] for new token i sets FORK_STATUS_BAD_DESC too;
- * pages stay taken and later calls of the step do nothing.  A page number
+ * pages stay taken and returned (blocks_out and ring_out hold) and later calls
+ * of the step do nothing.  A page number
  * outside [0, n_pages) sets FORK_STATUS_BAD_PAGE: its rows get slot -1 and are
  * not written (fork_cache_attn reads such a page as zeros).  Two launches, or one for up to 2048 rows
  * and 1024 requests.  Errors: FORK_EINVAL (null or misaligned pointers). */

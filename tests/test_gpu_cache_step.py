@@ -192,3 +192,61 @@ def test_steps_on_another_stream(F, torch):
         torch.cuda.synchronize()
         out.append((cr.attn_out["full"].clone(), token.clone(), cr.kv["full"][0].clone()))
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("T_cap", [40, 2100])  # the plan in one launch and in two
+@pytest.mark.parametrize("fault", ["parent", "page"])
+@pytest.mark.parametrize("call", ["keep", "status", "nothing"])
+def test_a_request_ends_in_a_step_that_fails(F, torch, T_cap, fault, call):
+    """The plan returned its pages before the step failed: its slot takes a new prompt, whatever is called in between."""
+    from tree_forked_hybrid_gb300 import workloads as wl
+    from tree_forked_hybrid_gb300.runner import CacheRound
+    cr = CacheRound((wl.AttnShape("full", 4, 2, 64, 0, 1e4),), T_cap=T_cap, max_req=3, max_new=20, max_blocks=4, n_pages=9, page_tokens=16)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    for x in cr.inputs["full"].values():
+        x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+    cr.plan(i32(20, 10, 3))
+    cr.run()
+    cr.keep([20, 10, 3])
+    parent = torch.full((T_cap,), -1, dtype=torch.int32)
+    state = [x.clone() for x in (*cr.kv["full"], cr.q_rot, cr.attn_out["full"])]
+    page = int(cr.cache.table[1, 0])
+    if fault == "parent":
+        parent[2] = 5
+    else:
+        cr.cache.table[1, 0] = 10 ** 6
+    cr.plan(i32(-1, 4, 0), parent)
+    cr.run()
+    if fault == "parent":  # what follows a refused tree does nothing
+        assert all(torch.equal(x, y) for x, y in zip(state, (*cr.kv["full"], cr.q_rot, cr.attn_out["full"])))
+    if call == "keep":
+        with pytest.raises(RuntimeError, match="BAD_DESC" if fault == "parent" else "BAD_PAGE"):
+            cr.keep([0, 1, 0], [[], [0], []])
+        assert cr.length.tolist() == [0, 10, 3]
+    elif call == "status":
+        assert cr.status() == (0x1 if fault == "parent" else F.FORK_STATUS_BAD_PAGE)
+    assert cr.blocks.tolist() == [0, 1, 1]
+    cr.cache.table[1, 0] = page
+    cr.plan(i32(18, 2, 1))
+    cr.run()
+    assert cr.status() == 0
+    assert to_np(cr.cache.kv_len).tolist() == [18, 12, 4] and to_np(cr.cache.tok_pos)[:21].tolist() == [*range(18), 10, 11, 3]
+    cr.keep([18, 2, 1])
+    assert cr.length.tolist() == [18, 12, 4]
+
+
+def test_a_request_ends_in_a_refused_step(F, torch):
+    """Refused as a whole: nothing went back, the length stays."""
+    cr = small_round(torch)
+    cr.plan(torch.tensor([3, 1], dtype=torch.int32))
+    cr.run()
+    cr.keep([3, 1])
+    cr.plan(torch.tensor([-1, 13], dtype=torch.int32))  # above max_new
+    with pytest.raises(RuntimeError, match="BAD_DESC"):
+        cr.keep([0, 0])
+    assert cr.length.tolist() == [3, 1] and cr.blocks.tolist() == [1, 1]
+    cr.plan(torch.tensor([1, 1], dtype=torch.int32))
+    cr.run()
+    cr.keep([1, 1])
+    assert cr.length.tolist() == [4, 2]

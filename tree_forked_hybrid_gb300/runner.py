@@ -531,15 +531,24 @@ class CacheRound:
         self.length, self.n_new, self.blocks = (torch.zeros(max_req, **i32) for _ in range(3))
         self.parent = torch.full((T_cap,), -1, **i32)
         self.ring, self.ring_state = torch.arange(n_pages, **i32), torch.tensor([0, n_pages], **i32)
+        self._open = False  # a step that `keep` has not closed
+
+    def _settle(self):
+        """Requests whose pages went back start again at length 0, also after a step that failed later on (one
+        refused as a whole returned none)."""
+        self.length.masked_fill_((self.n_new < 0) & (self.blocks == 0), 0)
 
     def plan(self, n_new: torch.Tensor, parent: Optional[torch.Tensor] = None, stream=None):
         """Tables of a step: new tokens per request [max_req] and, for trees, parents [T_cap]."""
         with torch.cuda.stream(stream):  # (None: the current one)
+            if self._open:
+                self._settle()
             self.n_new.copy_(n_new)
             if parent is not None:
                 self.parent.copy_(parent)
         F.fork_cache_plan(self.cache, self.length, self.n_new, None if parent is None else self.parent, self.blocks,
                           self.blocks, self.ring, self.ring_state, self.ring_state, stream=stream)
+        self._open = True
 
     def run(self, stream=None):
         """Every attention layer over the step's rows (``inputs`` -> ``attn_out``)."""
@@ -561,11 +570,13 @@ class CacheRound:
         """Keep n_keep[b] of the step's new tokens: the first ones of a chain, or those numbered
         path[b][:n_keep[b]] (ascending, each the parent of the next) of a tree, moved together.
         Host sequences.  Requests that have finished start again at length 0.  Raises, and keeps
-        nothing, after a step that raised a status bit; to be called on the step's stream."""
+        nothing, after a step that raised a status bit (a request whose pages went back has finished all
+        the same); to be called on the step's stream."""
         c = self.cache
         P = c.page_tokens
         status, n_new = self.status(), self.n_new.tolist()
         if status:
+            self._settle()
             raise RuntimeError("the step failed: " + ", ".join(n for b, n in F.STATUS_BITS.items() if status & b))
         if len(n_keep) != len(n_new) or any(not 0 <= k <= max(n, 0) for k, n in zip(n_keep, n_new)):
             raise ValueError("n_keep: from 0 up to the request's new tokens expected")
@@ -586,6 +597,7 @@ class CacheRound:
                     vc[tp, :, to] = vc[sp, :, so]
         self.length += torch.tensor(list(n_keep), dtype=torch.int32, device=c.device)
         self.length.masked_fill_(released, 0)
+        self._open = False
 
     def status(self) -> int:
         return F.fork_cache_status(self.cache)
