@@ -250,3 +250,39 @@ def test_a_request_ends_in_a_refused_step(F, torch):
     cr.run()
     cr.keep([1, 1])
     assert cr.length.tolist() == [4, 2]
+
+
+def test_keep_refuses_what_is_no_path(F, torch):
+    """Kept tokens have their keys rotated for the places that they are moved to only if they follow one another."""
+    cr = small_round(torch)
+    tree = torch.tensor([-1, 0, 0, 1, 3, -1, -1] + [-1] * 17, dtype=torch.int32)  # 0 -> (1 -> 3 -> 4, 2), 5; and a single one
+    cr.plan(torch.tensor([6, 1], dtype=torch.int32), tree)
+    cr.run()
+    for path in ([1, 0], [0, 0], [0, 1, 1], [1], [0, 3], [1, 3], [0, 2, 3], [0, 5], [0, 1, 2], [2, 0, 1]):
+        with pytest.raises(ValueError):
+            cr.keep([len(path), 0], [path, []])
+    for n in (3, 4):  # 0, 1, 2: the first tokens are not a path either
+        with pytest.raises(ValueError):
+            cr.keep([n, 0])
+    assert cr.length.tolist() == [0, 0]
+    k0, slot = cr.kv["full"][0].clone(), to_np(cr.cache.tok_slot)
+    cr.keep([4, 1], [(0, 1, 3, 4), np.array([0])])
+    assert cr.length.tolist() == [4, 1]
+    for to, was in enumerate((0, 1, 3, 4)):
+        a, b = divmod(int(slot[to]), 16), divmod(int(slot[was]), 16)
+        assert torch.equal(cr.kv["full"][0][a[0], :, a[1]], k0[b[0], :, b[1]])
+    # a chain after a tree: its first tokens alone (the parents of the step before do not count)
+    cr.plan(torch.tensor([4, 0], dtype=torch.int32))
+    cr.run()
+    for path in ([1], [0, 2], [1, 0], [0, 0]):
+        with pytest.raises(ValueError):
+            cr.keep([len(path), 0], [path, []])
+    cr.keep([3, 0], [[0, 1, 2, 3], []])
+    assert cr.length.tolist() == [7, 1]
+    # the first tokens of a tree that is a chain; 64 of them, the mask's last bit
+    from tree_forked_hybrid_gb300 import workloads as wl
+    from tree_forked_hybrid_gb300.runner import CacheRound
+    cr = CacheRound((wl.AttnShape("full", 4, 2, 64, 0, 1e4),), T_cap=70, max_req=1, max_new=64, max_blocks=8, n_pages=8, page_tokens=16)
+    cr.plan(torch.tensor([64], dtype=torch.int32), torch.arange(-1, 69, dtype=torch.int32))
+    cr.keep([64])
+    assert cr.length.tolist() == [64]

@@ -568,7 +568,8 @@ class CacheRound:
 
     def keep(self, n_keep, path=None):
         """Keep n_keep[b] of the step's new tokens: the first ones of a chain, or those numbered
-        path[b][:n_keep[b]] (ascending, each the parent of the next) of a tree, moved together.
+        path[b][:n_keep[b]] (each the parent of the next, the first a continuation of what was cached) of a
+        tree, moved together.  Anything else is refused: its keys were rotated for other positions.
         Host sequences.  Requests that have finished start again at length 0.  Raises, and keeps
         nothing, after a step that raised a status bit (a request whose pages went back has finished all
         the same); to be called on the step's stream."""
@@ -583,12 +584,21 @@ class CacheRound:
         if path is not None and any(len(path[b]) < k or any(not 0 <= i < n_new[b] for i in list(path[b])[:k])
                                     for b, k in enumerate(n_keep)):
             raise ValueError("path: numbers of the request's new tokens expected")
+        # a row's mask holds the numbers of its path (0 in a chain: all before it), so the last kept row's
+        # says which the others have to be
+        kept = [b for b, n in enumerate(n_keep) if n]
+        nodes = {b: list(range(n_keep[b])) if path is None else [int(i) for i in list(path[b])[:n_keep[b]]] for b in kept}
+        start = [0]
+        for n in n_new:
+            start.append(start[-1] + max(n, 0))
+        last = torch.tensor([start[b] + nodes[b][-1] for b in kept], dtype=torch.long)
+        for b, mask in zip(kept, c.tok_mask[last.to(c.device)].tolist()):
+            want = [i for i in range(F.FORK_CACHE_MAX_TREE) if mask >> i & 1] if mask else list(range(len(nodes[b])))
+            if nodes[b] != want:
+                raise ValueError("path: new tokens that follow one another expected")
         released = self.n_new < 0
         if path is not None:
-            start = c.row_start.tolist()
-            src = [start[b] + i for b, n in enumerate(n_keep) for i in list(path[b])[:n]]
-            dst = [start[b] + i for b, n in enumerate(n_keep) for i in range(n)]
-            moves = [(s, t) for s, t in zip(src, dst) if s != t]
+            moves = [(start[b] + i, start[b] + k) for b in kept for k, i in enumerate(nodes[b]) if i != k]
             if moves:
                 slots = c.tok_slot.long()[torch.tensor(moves, device=c.device).T]
                 (sp, tp), (so, to) = slots // P, slots % P
