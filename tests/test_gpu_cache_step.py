@@ -286,3 +286,27 @@ def test_keep_refuses_what_is_no_path(F, torch):
     cr.plan(torch.tensor([64], dtype=torch.int32), torch.arange(-1, 69, dtype=torch.int32))
     cr.keep([64])
     assert cr.length.tolist() == [64]
+
+
+def test_a_step_is_kept_once(F, torch):
+    cr = small_round(torch)
+    cr.plan(torch.tensor([3, 2], dtype=torch.int32))
+    cr.run()
+    cr.keep([2, 1])
+    for n_keep in ([1, 0], [2, 1], [0, 1]):
+        with pytest.raises(ValueError):
+            cr.keep(n_keep)
+    cr.keep([0, 0])
+    assert cr.length.tolist() == [2, 1]
+    # captured with the rest of a step: every replay is a step of its own
+    n_new = torch.tensor([1, 2], dtype=torch.int32).cuda()
+    cr.plan(n_new)
+    torch.cuda.synchronize()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        cr.plan(n_new)
+        cr.run()
+    for k in range(3):
+        gr.replay()
+        cr.keep([1, 2])
+        assert cr.length.tolist() == [3 + k, 3 + 2 * k]

@@ -572,7 +572,7 @@ class CacheRound:
         tree, moved together.  Anything else is refused: its keys were rotated for other positions.
         Host sequences.  Requests that have finished start again at length 0.  Raises, and keeps
         nothing, after a step that raised a status bit (a request whose pages went back has finished all
-        the same); to be called on the step's stream."""
+        the same).  A step is kept once: afterwards it has no new tokens.  To be called on the step's stream."""
         c = self.cache
         P = c.page_tokens
         status, n_new = self.status(), self.n_new.tolist()
@@ -607,6 +607,7 @@ class CacheRound:
                     vc[tp, :, to] = vc[sp, :, so]
         self.length += torch.tensor(list(n_keep), dtype=torch.int32, device=c.device)
         self.length.masked_fill_(released, 0)
+        self.n_new.zero_()  # (on the device: also between the replays of a captured plan)
         self._open = False
 
     def status(self) -> int:
