@@ -566,7 +566,8 @@ int fork_cache_append(const fork_cache* c, const fork_rope* rope, const uint16_t
  *   by one call at a time; nothing in it has to be set, nothing is kept.
  * The keys are read in tiles of 128, split over the GPU's SMs in equal shares;
  * what two SMs share of one row is joined in a fixed order, so a call's result
- * depends on the step's lengths but not on timing.  Two launches.
+ * depends on the step's lengths but not on timing.  Two launches.  A step with
+ * more than 2^30 tiles for one SM writes nothing and sets FORK_STATUS_CAPACITY.
  * Errors: FORK_EINVAL (null or misaligned pointers, window < 0, a scale that is
  * not positive and finite, a short workspace). */
 size_t fork_cache_attn_workspace_bytes(const fork_cache* c);

@@ -144,9 +144,17 @@ __device__ __forceinline__ bool cache_masked(const CacheAttnParams& p, const Cac
   return y0 + kKeyTile > all || (p.window > 0 && y0 <= last - p.window);
 }
 
+constexpr int kMaxRun = 1 << 30;  // tiles of one CTA, at most (the kernels count them in 32 bits)
+
+// x / y, mostly of small numbers (a 64-bit division takes some hundred cycles)
+__device__ __forceinline__ int64_t quotient_of(int64_t x, int64_t y) {
+  return (x | y) <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(x) / static_cast<uint32_t>(y)) : x / y;
+}
+
 // Where a CTA's run begins and ends: one warp counts the call's tiles, 32 items at a time (no
 // barrier: only the producers need it).  No run (begin == end) for CTAs beyond the tiles.
-// Runs differ by one tile at most: the first `more` CTAs have base + 1.
+// Runs differ by one tile at most: the first `more` CTAs have base + 1.  A call whose runs would be
+// longer than kMaxRun does nothing but raise FORK_STATUS_CAPACITY.
 struct CacheSplit {
   int head, item, off, n_item, base, more;
   int64_t begin, end;
@@ -155,13 +163,7 @@ struct CacheSplit {
 // CTA whose run holds the call's tile x
 __device__ __forceinline__ int cache_owner(const CacheSplit& s, int64_t x) {
   const int64_t wide = static_cast<int64_t>(s.more) * (s.base + 1);
-  if (x < wide) {
-    return wide <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(s.base + 1))
-                              : static_cast<int>(x / (s.base + 1));
-  }
-  const int64_t y = x - wide;
-  return s.more + (y <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(y) / static_cast<uint32_t>(s.base))
-                                   : static_cast<int>(y / s.base));
+  return static_cast<int>(x < wide ? quotient_of(x, s.base + 1) : s.more + quotient_of(x - wide, s.base));
 }
 
 __device__ __forceinline__ CacheSplit cache_split(const CacheAttnParams& p) {
@@ -172,28 +174,28 @@ __device__ __forceinline__ CacheSplit cache_split(const CacheAttnParams& p) {
   s.n_item = p.meta[C_NITEM];
   auto tiles = [&](int i) { return i < s.n_item ? cache_item(p, i).kt : 0; };
   const int v0 = lane < s.n_item ? first.kt : 0;
-  int per_head = v0;
+  int64_t per_head = v0;  // (131072 items of 8 tokens over 2.2 million cached ones: 2.8e9 tiles)
 #pragma unroll 4
   for (int i = 32 + lane; i < s.n_item; i += 32) per_head += tiles(i);
 #pragma unroll
   for (int k = 16; k > 0; k >>= 1) per_head += __shfl_xor_sync(0xffffffffu, per_head, k);
-  const int64_t total = static_cast<int64_t>(per_head) * p.Hkv;
+  const int64_t total = per_head * p.Hkv;
   const int ctas = static_cast<int>(total < gridDim.x ? total : gridDim.x);
   s.head = s.item = s.off = s.base = s.more = 0;
   s.begin = s.end = 0;
   const int c = blockIdx.x;
   if (c >= ctas) return s;
-  if (total <= 0x7fffffff) {  // (a 64-bit division takes some hundred cycles)
-    s.base = static_cast<int>(static_cast<uint32_t>(total) / static_cast<uint32_t>(ctas));
-  } else {
-    s.base = static_cast<int>(total / ctas);
+  const int64_t base_run = quotient_of(total, ctas);
+  if (base_run >= kMaxRun) {
+    if (lane == 0) atomicOr(p.meta + C_STATUS, FORK_STATUS_CAPACITY);
+    return s;
   }
+  s.base = static_cast<int>(base_run);
   s.more = static_cast<int>(total - static_cast<int64_t>(s.base) * ctas);
   s.begin = static_cast<int64_t>(s.base) * c + min(c, s.more);
   s.end = s.begin + s.base + (c < s.more ? 1 : 0);
-  s.head = s.begin <= 0x7fffffff ? static_cast<int>(static_cast<uint32_t>(s.begin) / static_cast<uint32_t>(per_head))
-                                 : static_cast<int>(s.begin / per_head);
-  int left = static_cast<int>(s.begin - static_cast<int64_t>(s.head) * per_head);  // tiles of this head before the run
+  s.head = static_cast<int>(quotient_of(s.begin, per_head));
+  int64_t left = s.begin - s.head * per_head;  // tiles of this head before the run
   for (int base = 0; base < s.n_item; base += 32) {
     const int v = base == 0 ? v0 : tiles(base + lane);
     int x = v;
@@ -206,7 +208,7 @@ __device__ __forceinline__ CacheSplit cache_split(const CacheAttnParams& p) {
     if (left < all) {
       const int at = __ffs(__ballot_sync(0xffffffffu, x > left)) - 1;
       s.item = base + at;
-      s.off = left - __shfl_sync(0xffffffffu, x - v, at);
+      s.off = static_cast<int>(left) - __shfl_sync(0xffffffffu, x - v, at);
       break;
     }
     left -= all;
