@@ -372,3 +372,25 @@ def test_an_infinity_that_every_row_sees(F, torch, max_new, d, what):
         for b in range(2):
             assert bool((got[b, :, 3 + b] == what).all())
             assert bool(torch.isfinite(got[b, :, :3 + b]).all()) and bool(torch.isfinite(got[b, :, 4 + b:]).all())
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,n,tree", [(4, 1, 128, 2, False), (16, 2, 64, 4, True), (16, 2, 128, 9, True), (8, 1, 64, 40, False)])
+def test_the_last_positions(F, torch, Hq, Hkv, d, n, tree):
+    """A windowed layer far along a stream, up to the last cache index that the handle allows (2^31 - 65): the bits of the
+    same step 2^31 - 2048 tokens earlier (pages before the window are not read)."""
+    P, far, W = 64, 2 ** 31 - 2048, 300
+    for end in (2048 - 64, 2048 - 64 - 70, 2048 - 128):  # the last tile half full, of one key or so, full
+        st = make_step(6, [end - n], [n], P, tree, n_pages=40)
+        q, kc, vc = inputs(torch, st, Hq, Hkv, d, 2)
+        want, _ = run(F, torch, st, q, kc, vc, Hq, Hkv, d, W)
+        check(torch, want, *reference(torch, st, q, kc, vc, W, d ** -0.5))
+        _, a = device_step(torch, st, Hq, Hkv, d)
+        c = F.Cache(st["T_cap"], 1, st["max_new"], (2 ** 31 - 1) // P, st["n_pages"], P, Hq, Hkv, d)
+        c.table[0, far // P:far // P + st["table"].shape[1]] = torch.from_numpy(st["table"][0]).cuda()
+        a["length"] += far
+        a["blocks_in"] += far // P
+        run_plan(F, c, a)
+        o = torch.zeros_like(q)
+        F.fork_cache_attn(c, q, kc, vc, o, W)
+        assert F.fork_cache_status(c) == 0
+        assert torch.equal(o[:n], want), end

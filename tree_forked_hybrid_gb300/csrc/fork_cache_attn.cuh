@@ -141,7 +141,7 @@ __device__ __forceinline__ bool cache_masked(const CacheAttnParams& p, const Cac
   const int y0 = t * kKeyTile;
   const int all = it.tree ? it.len : it.len + it.r0 + 1;  // every row sees the keys before (but for a window)
   const int last = it.len + it.r0 + it.nt - 1;                   // no row's position is higher
-  return y0 + kKeyTile > all || (p.window > 0 && y0 <= last - p.window);
+  return all - y0 < kKeyTile || (p.window > 0 && y0 <= last - p.window);
 }
 
 constexpr int kMaxRun = 1 << 30;  // tiles of one CTA, at most (the kernels count them in 32 bits)
