@@ -310,3 +310,21 @@ def test_a_step_is_kept_once(F, torch):
         gr.replay()
         cr.keep([1, 2])
         assert cr.length.tolist() == [3 + k, 3 + 2 * k]
+
+
+def test_plan_refuses_other_shapes(F, torch):
+    """One count for every request and one parent for every row; nothing is spread or cut silently."""
+    cr = small_round(torch)
+    cr.plan(torch.tensor([3, 1], dtype=torch.int32))
+    cr.run()
+    cr.keep([3, 1])
+    for n_new, parent in ((torch.tensor([1]), None), (torch.tensor(1), None), (torch.tensor([[1, 1]]), None), (torch.tensor([1.5, 1.0]), None),
+                          (torch.tensor([1, 1, 1]), None), (torch.tensor([1, 1]), torch.tensor([-1])),
+                          (torch.tensor([1, 1]), torch.full((25,), -1)), (torch.tensor([1, 1]), torch.full((24,), -1.0))):
+        with pytest.raises(ValueError):
+            cr.plan(n_new, parent)
+    assert cr.n_new.tolist() == [0, 0] and cr.length.tolist() == [3, 1]
+    cr.plan(torch.tensor([2, 1]), torch.tensor([-1, 0] + [-1] * 22))  # (64-bit counts and parents do)
+    cr.run()
+    cr.keep([2, 1])
+    assert cr.length.tolist() == [5, 2]

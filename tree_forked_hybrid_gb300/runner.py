@@ -539,7 +539,10 @@ class CacheRound:
         self.length.masked_fill_((self.n_new < 0) & (self.blocks == 0), 0)
 
     def plan(self, n_new: torch.Tensor, parent: Optional[torch.Tensor] = None, stream=None):
-        """Tables of a step: new tokens per request [max_req] and, for trees, parents [T_cap]."""
+        """Tables of a step: new tokens per request [max_req] and, for trees, parents [T_cap] (whole numbers)."""
+        for name, x, own in (("n_new", n_new, self.n_new), ("parent", parent, self.parent)):
+            if x is not None and (x.shape != own.shape or x.is_floating_point()):
+                raise ValueError(f"{name}: whole numbers {tuple(own.shape)} expected, got {x.dtype} {tuple(x.shape)}")
         with torch.cuda.stream(stream):  # (None: the current one)
             if self._open:
                 self._settle()
