@@ -22,8 +22,9 @@ enum CacheHdr : int {
 // request can have in a step, because the launch may not read the device.  16 rows, and 32 of
 // heads of 64, go to the kernel on warp-level products, more to the tcgen05 one (128, or 256 in
 // two tiles).  Measured, warp-level / tcgen05: 64 requests x 1 token x 4 heads of 128 (0.95 GB)
-// 148 / 160 us; with 32-row items, 32 requests x 8 tokens x 4 heads of 128 116 / 94 us, but of 64
-// (64 requests) 99 / 129 us, and 32 requests of 2 to 8 tokens x 3 heads of 64 21 / 29 us.
+// 147 / 160 us; with 32-row items, 32 requests x 8 tokens x 4 heads of 128 116 / 94 us (when both were
+// timed), but of 64 (64 requests) 107 / 129 us, and 32 requests of 2 to 8 tokens x 3 heads of 64
+// 22.5 / 29 us.
 __host__ __device__ inline int cache_item_rows(int max_new, int G, int d) {
   const int64_t most = static_cast<int64_t>(max_new) * G;
   return most <= 16 ? 16 : (most <= 32 && d == 64 ? 32 : (most <= 128 / G * G ? 128 : 256));

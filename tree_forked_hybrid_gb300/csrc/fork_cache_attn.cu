@@ -10,12 +10,13 @@
 // ends, when they are joined in shared memory.  One more warp fetches the next piece's queries
 // and what its rows see while this one is worked on (in the consumers' own time that was 2000
 // to 2500 of the 24000 cycles of a small call).  The maximum of a row only moves when a score
-// exceeds it by 2^8: the usual tile needs one vote instead of shuffles and a rescaling.  Products on mma.sync m16n8k16: 16 or 32 query
-// rows would fill an eighth or a quarter of a 128-row tcgen05 tile, and registers take the
-// exponentials without a trip through tensor memory.
-// 64 requests x 1 token x 4 heads of 128 (0.95 GB): 148 us, 0.96 of the measured HBM rate.  Of 64
-// (half the bytes of a tile for the same latencies; 64 requests x 8 x 4): 99 us.  A call of one
-// request and one short tile: 9 us, the latency of the tables, the queries and the first tile.
+// exceeds it by 2^8: the usual tile needs one vote instead of shuffles and a rescaling.  Products
+// on mma.sync m16n8k16: 16 or 32 query rows would fill an eighth or a quarter of a 128-row tcgen05
+// tile, and registers take the exponentials without a trip through tensor memory.
+// 64 requests x 1 token x 4 heads of 128 over 1,000 to 6,000 keys (0.95 GB): 145 us, 0.98 of the
+// measured HBM rate.  Of 64 (half the bytes of a tile for the same latencies; 64 requests x 8 x 4,
+// 0.48 GB): 107 us.  A call of one request and a few short tiles: 9.6 us, the latency of the
+// tables, the queries and the first tile.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -351,9 +352,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // A weight goes into the product as two bf16 numbers, to 2^-15 of it: the largest below it
           // and the rest, both positive (times an infinite value they do not make a NaN);
           // the sum takes it in float32.  The second product is hidden by the wait for HBM where there
-          // is one: 64 requests x 1 token x 4 heads of 128 147 us (rounded to one bf16 number 147.6),
-          // heads of 64 with one kv head 25.4 (24.1), small trees over a window 22.1 (21.3).  The
-          // relative error against 64 bits is 0.0017, the rounding of the result (0.0020)
+          // is one: 64 requests x 1 token x 4 heads of 128 143.3 us (rounded to one bf16 number
+          // 142.5), of 64 86.1 (85.0), small trees of 27 rows over a window 22.5 (21.6), 64 requests x
+          // 32 rows of heads of 64 106.5 (97.3).  The relative error against 64 bits is 0.0017, the
+          // rounding of the result (0.0020)
           const float at = mx[h] == -INFINITY ? 0.f : mx[h];
 #pragma unroll
           for (int g = 0; g < MT; ++g) {

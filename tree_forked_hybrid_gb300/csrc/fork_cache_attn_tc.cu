@@ -17,8 +17,9 @@
 //               row sees, running maximum (moved only when it grows by more than 2^8, so
 //               that O is rescaled rarely), exponentials as bf16 into the columns of S, from
 //               where the PV product reads them; at the end O / l or a partial result
-// 131,000 keys x 256 rows (8 kv heads of 128; 538 MB, 137 GFLOP): 133 us, 0.60 of the measured HBM
-// rate and 0.54 of the measured tensor rate at once; bound by the turn of softmax and products
+// 131,000 keys x 256 rows (8 kv heads of 128; 538 MB, 137 GFLOP): 133 us back to back (135 to 138
+// among other calls), 0.60 of the measured HBM rate and 0.54 of the measured tensor rate at once;
+// bound by the turn of softmax and products
 // (without exponentials 113 us, without copies 143 of then 148, without both 107).  16 requests x
 // 64 nodes: 99 us, 839 TFLOP/s.  32 requests x 8 nodes x 4 heads of 128 (0.53 GB): 94 us, 5.6 TB/s.
 // TMEM: S_t / P_t at columns 128 t, O_t at 256 + t D.  QK^T and PV in bf16 with float32 sums.

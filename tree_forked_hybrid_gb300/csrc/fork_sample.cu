@@ -27,9 +27,10 @@
 // 512 rows of 131072 floats (normal, sigma 2, and 24 that stand out), thousands of cycles of a
 // row: the maximum 29 (HBM), a list of candidates 28 (L2), all weights 62 to 70 (some 45
 // instructions a token), bins of light weights 85 (two shared-memory atomics a token).  Greedy
-// 65 us (4.1 TB/s), top-k 126, min-p 113, none 197; top-p 0.9 at temperature 0.5 (the cut among
-// the listed) 215 to 230, at 0.9 (some rows' cut among light tokens) 455; all kinds mixed 155 to
-// 174, by the draw of the kinds.
+// 62 to 65 us (4.2 TB/s), top-k 127, min-p 113, none 197; top-p 0.9 at temperature 0.5 (the cut
+// among the listed) 212 to 230, at 0.9 (some rows' cut among light tokens) 454, at 1.3 604; all kinds
+// mixed 155 to 174, by the draw of the kinds.  Other rows, top-p 0.9 at 0.9: normal of sigma 4 363, of
+// sigma 1 842, Laplace of scale 2 215, uniform over 20 628, all equal 6057 (atomics at one address).
 #include <algorithm>
 #include <cmath>
 
