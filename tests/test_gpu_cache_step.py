@@ -323,8 +323,25 @@ def test_plan_refuses_other_shapes(F, torch):
                           (torch.tensor([1, 1]), torch.full((25,), -1)), (torch.tensor([1, 1]), torch.full((24,), -1.0))):
         with pytest.raises(ValueError):
             cr.plan(n_new, parent)
-    assert cr.n_new.tolist() == [0, 0] and cr.length.tolist() == [3, 1]
+    assert cr.n_new.tolist() == [3, 1] and cr.length.tolist() == [3, 1]
     cr.plan(torch.tensor([2, 1]), torch.tensor([-1, 0] + [-1] * 22))  # (64-bit counts and parents do)
     cr.run()
     cr.keep([2, 1])
     assert cr.length.tolist() == [5, 2]
+
+
+def test_the_rounds_own_counts_are_planned_again(F, torch):
+    """n_new filled once, a captured plan of it replayed: a token for every request in every step."""
+    cr = small_round(torch)
+    cr.n_new.fill_(1)
+    cr.plan(cr.n_new)
+    cr.run()
+    cr.keep([1, 1])
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        cr.plan(cr.n_new)
+        cr.run()
+    for k in range(4):
+        gr.replay()
+        cr.keep([1, 1])
+        assert cr.length.tolist() == [2 + k, 2 + k] and cr.n_new.tolist() == [1, 1]

@@ -528,7 +528,9 @@ class CacheRound:
         self.q_rot = torch.zeros((T_cap, a0.Hq, a0.d), **bf)
         self.ws = torch.empty(F.fork_cache_attn_workspace_bytes(self.cache), dtype=torch.uint8, device=device)
         i32 = dict(dtype=torch.int32, device=dev)
-        self.length, self.n_new, self.blocks = (torch.zeros(max_req, **i32) for _ in range(3))
+        # (_step: the counts of the step that `keep` has not closed; n_new may be the caller's own buffer, filled and
+        # passed to `plan` in every step)
+        self.length, self.n_new, self.blocks, self._step = (torch.zeros(max_req, **i32) for _ in range(4))
         self.parent = torch.full((T_cap,), -1, **i32)
         self.ring, self.ring_state = torch.arange(n_pages, **i32), torch.tensor([0, n_pages], **i32)
         self._open = False  # a step that `keep` has not closed
@@ -536,7 +538,7 @@ class CacheRound:
     def _settle(self):
         """Requests whose pages went back start again at length 0, also after a step that failed later on (one
         refused as a whole returned none)."""
-        self.length.masked_fill_((self.n_new < 0) & (self.blocks == 0), 0)
+        self.length.masked_fill_((self._step < 0) & (self.blocks == 0), 0)
 
     def plan(self, n_new: torch.Tensor, parent: Optional[torch.Tensor] = None, stream=None):
         """Tables of a step: new tokens per request [max_req] and, for trees, parents [T_cap] (whole numbers)."""
@@ -547,6 +549,7 @@ class CacheRound:
             if self._open:
                 self._settle()
             self.n_new.copy_(n_new)
+            self._step.copy_(self.n_new)
             if parent is not None:
                 self.parent.copy_(parent)
         F.fork_cache_plan(self.cache, self.length, self.n_new, None if parent is None else self.parent, self.blocks,
@@ -578,7 +581,7 @@ class CacheRound:
         the same).  A step is kept once: afterwards it has no new tokens.  To be called on the step's stream."""
         c = self.cache
         P = c.page_tokens
-        status, n_new = self.status(), self.n_new.tolist()
+        status, n_new = self.status(), self._step.tolist()
         if status:
             self._settle()
             raise RuntimeError("the step failed: " + ", ".join(n for b, n in F.STATUS_BITS.items() if status & b))
@@ -599,7 +602,7 @@ class CacheRound:
             want = [i for i in range(F.FORK_CACHE_MAX_TREE) if mask >> i & 1] if mask else list(range(len(nodes[b])))
             if nodes[b] != want:
                 raise ValueError("path: new tokens that follow one another expected")
-        released = self.n_new < 0
+        released = self._step < 0
         if path is not None:
             moves = [(start[b] + i, start[b] + k) for b in kept for k, i in enumerate(nodes[b]) if i != k]
             if moves:
@@ -610,7 +613,7 @@ class CacheRound:
                     vc[tp, :, to] = vc[sp, :, so]
         self.length += torch.tensor(list(n_keep), dtype=torch.int32, device=c.device)
         self.length.masked_fill_(released, 0)
-        self.n_new.zero_()  # (on the device: also between the replays of a captured plan)
+        self._step.zero_()  # (on the device: also between the replays of a captured plan)
         self._open = False
 
     def status(self) -> int:
