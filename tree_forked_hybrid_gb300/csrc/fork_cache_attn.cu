@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        uint32_t pf[MT][4], pr[MT][4];  // bf16, and what the rounding left
+        uint32_t pf[MT][4], pr[MT][4];  // two bf16 numbers per weight
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           // A weight goes into the product as two bf16 numbers, to 2^-15 of it: the largest below it
